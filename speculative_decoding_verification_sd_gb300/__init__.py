@@ -20,6 +20,7 @@ for convenience.  PyTorch provides device memory and streams, nothing else.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 from typing import Optional
@@ -80,6 +81,17 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _filling(stream):
+    """Context in which torch allocates and fills on the stream that the call is given:
+    fills are in order before the kernel, and memory that the call lets go of is handed
+    out again behind it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):  # 0, and 1 by name: the default stream
+        stream = torch.cuda.default_stream() if stream in (0, 1) else torch.cuda.ExternalStream(stream)
+    return torch.cuda.stream(stream)
 
 
 def _dt(dt):
@@ -192,7 +204,9 @@ def verify_workspace(bs: int, k_max: int, V: int, dt, device=None) -> torch.Tens
 
 
 # ---------------------------------------------------------------------------
-# Convenience layer: allocate outputs with torch and call the C ABI.
+# Convenience layer: allocate outputs with torch and call the C ABI.  What is
+# allocated here belongs to `stream`, as if the call stood under
+# torch.cuda.stream(stream); inputs have to be ready on it.
 
 
 @dataclass
@@ -219,18 +233,19 @@ def plan(draft_lens: torch.Tensor, k_max: int, conf: Optional[torch.Tensor] = No
          stream=None) -> PlanResult:
     dev = draft_lens.device
     bs = draft_lens.numel()
-    B = torch.empty(1, dtype=torch.int32, device=dev)
-    mask = torch.empty((bs, max(k_max, 1)), dtype=torch.uint8, device=dev)
-    nv = torch.empty(bs, dtype=torch.int32, device=dev)
-    cu = torch.empty(bs + 1, dtype=torch.int32, device=dev)
-    if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=dev)
     bsb = 0 if budget_draft_lens is None else budget_draft_lens.numel()
-    # an empty packed array is still a valid (unread) buffer for the C ABI
-    if conf is not None and conf.numel() == 0:
-        conf = torch.zeros(1, dtype=torch.float32, device=dev)
-    if budget_conf is not None and budget_conf.numel() == 0:
-        budget_conf = torch.zeros(1, dtype=torch.float32, device=dev)
+    with _filling(stream):
+        B = torch.empty(1, dtype=torch.int32, device=dev)
+        mask = torch.empty((bs, max(k_max, 1)), dtype=torch.uint8, device=dev)
+        nv = torch.empty(bs, dtype=torch.int32, device=dev)
+        cu = torch.empty(bs + 1, dtype=torch.int32, device=dev)
+        if err is None:
+            err = torch.zeros(1, dtype=torch.int32, device=dev)
+        # an empty packed array is still a valid (unread) buffer for the C ABI
+        if conf is not None and conf.numel() == 0:
+            conf = torch.zeros(1, dtype=torch.float32, device=dev)
+        if budget_conf is not None and budget_conf.numel() == 0:
+            budget_conf = torch.zeros(1, dtype=torch.float32, device=dev)
     sd_plan(conf, budget_conf, budget_draft_lens, bsb, draft_lens, bs, k_max, cost,
             0 if cost is None else cost.numel(), T, mode, B, mask, nv, cu, err, None, 0, stream)
     return PlanResult(B, mask[:, :k_max], nv, cu, err)
@@ -243,13 +258,14 @@ def verify(target: torch.Tensor, draft: Optional[torch.Tensor], dt, V: int,
            cfg=None, stream=None) -> VerifyResult:
     dev = target.device
     bs = cu_seqlens.numel() - 1
-    acc = torch.empty(bs, dtype=torch.int32, device=dev)
-    out = torch.empty((bs, k_max + 1), dtype=torch.int32, device=dev)
-    pr = torch.full((max(bs * k_max, 1), 2), float("nan"), dtype=torch.float32, device=dev) if probs else None
-    if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=dev)
-    if workspace is None:
-        workspace = verify_workspace(bs, k_max, V, dt, dev)
+    with _filling(stream):
+        acc = torch.empty(bs, dtype=torch.int32, device=dev)
+        out = torch.empty((bs, k_max + 1), dtype=torch.int32, device=dev)
+        pr = torch.full((max(bs * k_max, 1), 2), float("nan"), dtype=torch.float32, device=dev) if probs else None
+        if err is None:
+            err = torch.zeros(1, dtype=torch.int32, device=dev)
+        if workspace is None:
+            workspace = verify_workspace(bs, k_max, V, dt, dev)
     sd_verify_ex(target, draft, dt, V, draft_ids, uniforms, temps, cu_seqlens, bs, k_max, acc,
                  out, pr, err, workspace, workspace.numel(), cfg=cfg, stream=stream)
     return VerifyResult(acc, out, pr, err)
@@ -401,7 +417,8 @@ def append(k_new: torch.Tensor, v_new: torch.Tensor, cache: KVCache, cu_seqlens:
     if k_new.shape[0] < bs * (k_max + 1):
         raise ValueError(f"rows for {bs} requests of up to {k_max + 1} are needed")
     if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=cache.k.device)
+        with _filling(stream):
+            err = torch.zeros(1, dtype=torch.int32, device=cache.k.device)
     sd_cache_append(ka, va, ks, cache, cu_seqlens, kv_lens, bs, k_max, err, stream)
     return err
 
@@ -422,20 +439,21 @@ def attend(q: torch.Tensor, cache: KVCache, cu_seqlens: torch.Tensor, kv_lens: t
     qa, qs = _rows(q, q_heads, cache.head_dim)
     if rows < bs * (k_max + 1):
         raise ValueError(f"rows for {bs} requests of up to {k_max + 1} are needed")
-    if out is None:
-        out = torch.zeros((rows, q_heads, dim), dtype=torch.bfloat16, device=q.device)
-    if lse is True:
-        lse = torch.zeros((rows, q_heads), dtype=torch.float32, device=q.device)
+    with _filling(stream):
+        if out is None:
+            out = torch.zeros((rows, q_heads, dim), dtype=torch.bfloat16, device=q.device)
+        if lse is True:
+            lse = torch.zeros((rows, q_heads), dtype=torch.float32, device=q.device)
+        if err is None:
+            err = torch.zeros(1, dtype=torch.int32, device=q.device)
+        if workspace is None:
+            workspace = attend_workspace(bs, k_max, q_heads, cache)
     lse = None if lse is False else lse
     if out.dtype != _BF16 or out.dim() != 3 or out.shape[1:] != q.shape[1:] or out.shape[0] < bs * (k_max + 1):
         raise ValueError(f"out must be bf16 [at least {bs * (k_max + 1)}, {q_heads}, {dim}]")
     if lse is not None and (lse.dtype != _F32 or lse.dim() != 2 or lse.shape[1] != q_heads or
                             lse.shape[0] < bs * (k_max + 1)):
         raise ValueError(f"lse must be fp32 [at least {bs * (k_max + 1)}, {q_heads}]")
-    if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=q.device)
-    if workspace is None:
-        workspace = attend_workspace(bs, k_max, q_heads, cache)
     sd_attend(qa, qs, q_heads, cache, cu_seqlens, kv_lens, bs, k_max,
               dim ** -0.5 if scale is None else scale, out, lse, err, workspace, workspace.numel(),
               stream)
@@ -466,16 +484,17 @@ def sample(logits: torch.Tensor, temps: torch.Tensor, uniforms: Optional[torch.T
     if uniforms is None:
         if tokens is not None:
             raise ValueError("tokens are drawn from uniforms: pass both or neither")
-    elif tokens is None:
-        tokens = torch.zeros(rows, dtype=torch.int32, device=logits.device)
+    with _filling(stream):
+        if uniforms is not None and tokens is None:
+            tokens = torch.zeros(rows, dtype=torch.int32, device=logits.device)
+        if kept is True:
+            kept = torch.zeros_like(logits)
+        if err is None:
+            err = torch.zeros(1, dtype=torch.int32, device=logits.device)
     _need(tokens, "tokens", _I32, rows)
-    if kept is True:
-        kept = torch.zeros_like(logits)
     kept = None if kept is False else kept
     if kept is not None and (kept.shape != logits.shape or kept.dtype != logits.dtype):
         raise ValueError("kept must have the logits' shape and dtype")
-    if err is None:
-        err = torch.zeros(1, dtype=torch.int32, device=logits.device)
     sd_sample(logits, logits.dtype, V, rows, cu_seqlens, bs, temps, top_k, top_p, min_p, uniforms,
               tokens, kept, err, stream)
     return SampleResult(tokens, kept, err)

@@ -1,0 +1,127 @@
+"""append, attend, sample, plan and verify through their ``stream`` argument
+with nothing handed over."""
+
+import pytest
+
+import serving_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import speculative_decoding_verification_sd_gb300 as sd  # noqa: E402
+from test_gpu_cache_attend import device_cache  # noqa: E402
+
+i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+
+
+def hold(seconds=0.2):
+    """Keeps the current stream busy for about that long."""
+    torch.cuda._sleep(int(seconds * 2e9))
+
+
+def attend_inputs(lens=(5000, 20000, 300), counts=(3, 1, 8), seed=0):
+    """A step whose segments are cut by the shares' borders."""
+    g = torch.Generator().manual_seed(seed)
+    k, v, table, _, _ = ref.make_cache(g, list(lens), 16, 2, 128)
+    q = torch.randn((len(lens) * 8, 8, 128), generator=g).bfloat16().cuda()
+    return q, device_cache(k, v, table, None, None), torch.tensor(ref.compaction(counts)).cuda(), i32(list(lens)), 7
+
+
+@pytest.fixture(params=["stream", "handle"])
+def side(request):
+    s = torch.cuda.Stream()
+    return s, s if request.param == "stream" else s.cuda_stream
+
+
+def test_attend_fills_on_the_calls_stream(side):
+    s, arg = side
+    a = attend_inputs()
+    used = int(a[2][-1])
+    want = sd.attend(*a, lse=True)
+    torch.cuda.synchronize()
+    hold()
+    r = sd.attend(*a, lse=True, stream=arg)
+    torch.cuda.synchronize()
+    assert torch.equal(r.out, want.out) and torch.equal(r.lse, want.lse) and int(r.err) == 0
+    assert not r.out[used:].any()
+    bad = i32([5000, -1, 300])
+    hold()
+    r = sd.attend(*a[:3], bad, 7, stream=arg)
+    torch.cuda.synchronize()
+    assert int(r.err) == sd.SD_DEV_ERR_CACHE
+
+
+def test_attends_own_workspace_lives_until_the_call_is_done(side):
+    s, arg = side
+    a = attend_inputs()
+    want = sd.attend(*a)
+    n = sd.sd_attend_workspace_bytes(3, 7, 8, 2, 128)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(s):
+        hold()
+    r = sd.attend(*a, stream=arg)
+    junk = torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # a freed workspace's place, if there is one
+    torch.cuda.synchronize()
+    assert torch.equal(r.out, want.out) and int(r.err) == 0 and int(junk[0]) == 255
+
+
+def test_append_raises_its_bit_on_the_calls_stream(side):
+    _, arg = side
+    _, cache, cu, lens, k_max = attend_inputs()
+    new, bad = torch.zeros((24, 2, 128), dtype=torch.bfloat16, device="cuda"), i32([5000, -1, 300])
+    sd.append(new, new, cache, cu, bad, k_max)  # (loading a kernel would wait for the held stream)
+    torch.cuda.synchronize()
+    hold()
+    err = sd.append(new, new, cache, cu, bad, k_max, stream=arg)
+    torch.cuda.synchronize()
+    assert int(err) == sd.SD_DEV_ERR_CACHE
+
+
+def test_sample_fills_on_the_calls_stream(side):
+    _, arg = side
+    z = torch.randn((9, 5000), generator=torch.Generator().manual_seed(1)).cuda()
+    t, u, k = torch.ones(9).cuda(), torch.linspace(0.0, 0.9, 9).cuda(), torch.full((9,), 30, dtype=torch.int32).cuda()
+    want = sd.sample(z, t, u, k, kept=True)
+    torch.cuda.synchronize()
+    assert bool(want.tokens.any())
+    hold()
+    r = sd.sample(z, t, u, k, kept=True, stream=arg)
+    torch.cuda.synchronize()
+    assert torch.equal(r.tokens, want.tokens) and torch.equal(r.kept, want.kept) and int(r.err) == 0
+    t.neg_()
+    torch.cuda.synchronize()
+    hold()
+    r = sd.sample(z, t, u, stream=arg)
+    torch.cuda.synchronize()
+    assert int(r.err) == sd.SD_DEV_ERR_TEMP
+
+
+def test_plan_raises_its_bit_on_the_calls_stream(side):
+    _, arg = side
+    lens = i32([3, 99, 2])
+    sd.plan(lens, 4, mode=sd.SD_MODE_ALL_SLOTS)
+    torch.cuda.synchronize()
+    hold()
+    r = sd.plan(lens, 4, mode=sd.SD_MODE_ALL_SLOTS, stream=arg)
+    torch.cuda.synchronize()
+    assert int(r.err) == sd.SD_DEV_ERR_DRAFT_LENS
+
+
+def test_verify_fills_on_the_calls_stream(side):
+    _, arg = side
+    bs, k, V = 5, 3, 4000
+    g = torch.Generator().manual_seed(2)
+    z, y = torch.randn((bs * (k + 1), V), generator=g).cuda(), torch.randn((bs * k, V), generator=g).cuda()
+    ids, u = torch.randint(0, V, (bs * k,), generator=g).int().cuda(), torch.rand((bs, k + 1), generator=g).cuda()
+    cu, t = i32(list(range(0, bs * (k + 1) + 1, k + 1))), torch.ones(bs).cuda()
+    want = sd.verify(z, y, sd.SD_F32, V, ids, u, t, cu, k, probs=True)
+    torch.cuda.synchronize()
+    hold()
+    r = sd.verify(z, y, sd.SD_F32, V, ids, u, t, cu, k, probs=True, stream=arg)
+    torch.cuda.synchronize()
+    assert torch.equal(r.out_tokens, want.out_tokens) and torch.equal(r.accepted_len, want.accepted_len)
+    assert torch.equal(torch.nan_to_num(r.probs), torch.nan_to_num(want.probs)) and int(r.err) == 0
