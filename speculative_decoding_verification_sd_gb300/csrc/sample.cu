@@ -46,8 +46,10 @@
 // 362 us are 1.65 TB/s, a quarter of the copy rate.
 #include <cooperative_groups.h>
 
+#include <atomic>
 #include <cfloat>
 #include <cmath>
+#include <mutex>
 
 #include "f32x2.cuh"
 #include "serving.h"
@@ -1419,6 +1421,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   cluster.sync();  // no CTA leaves while another may still read its shared memory
 }
 
+// Raises the kernel's dynamic shared-memory limit to the device's, once per
+// device: the limit belongs to the kernel, not to a launch, so a call that set
+// its own size would refuse another thread's larger one.
+template <typename T>
+cudaError_t shared_limit(int* limit) {
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> limit_of[kMaxDev];
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidValue;
+  *limit = limit_of[dev].load(std::memory_order_acquire);
+  if (*limit != 0) return cudaSuccess;
+  std::lock_guard<std::mutex> lock(mu);
+  int optin = 0;
+  cudaFuncAttributes fa;
+  e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, sample_kernel<T>);
+  if (e != cudaSuccess) return e;
+  const int most = optin - static_cast<int>(fa.sharedSizeBytes);
+  e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e != cudaSuccess) return e;
+  limit_of[dev].store(most, std::memory_order_release);
+  *limit = most;
+  return cudaSuccess;
+}
+
 constexpr int kFewCtas = 76;  // half the SMs: twice as many CTAs still run side by side
 
 template <typename T>
@@ -1436,9 +1466,10 @@ cudaError_t launch(SampleParams& p, cudaStream_t s) {
   const int slice_vecs = (vecs + C - 1) / C;
   p.slice = slice_vecs * N;
   const size_t smem = static_cast<size_t>(slice_vecs) * 16;
-  cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  int limit = 0;
+  cudaError_t e = shared_limit<T>(&limit);
   if (e != cudaSuccess) return e;
+  if (smem > static_cast<size_t>(limit)) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = C;

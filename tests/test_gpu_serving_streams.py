@@ -1,5 +1,6 @@
 """append, attend, sample, plan and verify through their ``stream`` argument
-with nothing handed over."""
+with nothing handed over, and the calls from several host threads."""
+import threading
 
 import pytest
 
@@ -125,3 +126,66 @@ def test_verify_fills_on_the_calls_stream(side):
     torch.cuda.synchronize()
     assert torch.equal(r.out_tokens, want.out_tokens) and torch.equal(r.accepted_len, want.accepted_len)
     assert torch.equal(torch.nan_to_num(r.probs), torch.nan_to_num(want.probs)) and int(r.err) == 0
+
+
+def both(*work, times):
+    """Runs the functions in a thread each, on streams of their own; raises what one of them raised."""
+    failed, ready = [], threading.Barrier(len(work))
+
+    def loop(fn):
+        try:
+            s = torch.cuda.Stream()
+            ready.wait()
+            for _ in range(times):
+                fn(s)
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=loop, args=(fn,)) for fn in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    if failed:
+        raise failed[0]
+
+
+def test_threads_sample_rows_of_other_lengths():
+    """Through the C entry, whose calls run side by side (ctypes lets go of the interpreter)."""
+    lib = sd._lib.load()
+
+    def rows(V):
+        g = torch.Generator().manual_seed(V)
+        z, t, u = torch.randn((1, V), generator=g).cuda(), torch.ones(1).cuda(), torch.rand(1, generator=g).cuda()
+        want = sd.sample(z, t, u).tokens.clone()
+        got, err = torch.zeros_like(want), torch.zeros(1, dtype=torch.int32, device="cuda")
+        at = [x.data_ptr() for x in (z, t, u, got, err)]
+
+        def call(s):
+            st = lib.sd_sample(at[0], sd.SD_F32, V, 1, None, 1, at[1], None, None, None, at[2], at[3], None, at[4],
+                               s.cuda_stream)
+            if st != sd.SD_OK:
+                raise AssertionError(f"V={V}: {st} {lib.sd_last_error_string()}")
+        return call, got, want, err, z, t, u
+
+    cases = [rows(256000), rows(1000), rows(200000), rows(64)]
+    torch.cuda.synchronize()
+    both(*(c[0] for c in cases), times=10000)
+    for _, got, want, err, *_ in cases:
+        assert torch.equal(got, want) and int(err) == 0
+
+
+def test_threads_attend_with_a_workspace_each():
+    def step(seed, lens, counts):
+        q, cache, cu, lens, k_max = attend_inputs(lens, counts, seed)
+        want = sd.attend(q, cache, cu, lens, k_max).out.clone()
+        got, err = torch.zeros_like(want), torch.zeros(1, dtype=torch.int32, device="cuda")
+        ws = sd.attend_workspace(cu.numel() - 1, k_max, 8, cache)
+        return (lambda s: sd.attend(q, cache, cu, lens, k_max, out=got, err=err, workspace=ws, stream=s)), got, want, err
+
+    a, b = step(1, (5000, 20000, 300), (3, 1, 8)), step(2, (900, 7, 40, 30000), (1, 2, 8, 1))
+    torch.cuda.synchronize()
+    both(a[0], b[0], times=300)
+    for _, got, want, err in (a, b):
+        assert torch.equal(got, want) and int(err) == 0
