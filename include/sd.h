@@ -429,9 +429,9 @@ sd_status sd_cache_append(const void* k_new, const void* v_new, long long row_st
  *              SD_DEV_ERR_TIMEOUT: a wait inside the kernel gave up; out and
  *              lse_out are undefined and the workspace has to be zero-filled
  *              again.
- * Slots at or beyond kv_lens[i] are never used, whatever they hold.  A
- * non-finite value in a visible key or value row reaches every row of the
- * step that shares its cache head.  Results do not depend on timing: partial
+ * Slots at or beyond kv_lens[i] are never used, whatever they hold, and a row
+ * takes nothing from tokens that it does not see: a non-finite key or value of
+ * a late token of the step leaves the rows before it as they are.  Results do not depend on timing: partial
  * sums are joined in a fixed order.
  * Limits: as sd_cache_append, q_heads a multiple of heads, q_heads / heads <= SD_MAX_HEAD_GROUP, |scale| finite. */
 #define SD_MAX_HEAD_GROUP 128

@@ -116,6 +116,10 @@ struct Shared {
   int start_i;                    // first request of this CTA's share ...
   long long start_off, u0, u1, total;  // ... and the unit within it; the share; all units
   int last;                       // this CTA joins a segment's parts
+  // A byte per softmax warp: it took non-finite values out of the segment's tiles.
+  // Four buffers: while segment k's rows go out, O of k + 2 has not been started, so
+  // the weights are at most two tiles into it, in k + 3.
+  uint64_t odd[4];
   float tile_m[2][2][128];        // maxima of the halves of a lane's tokens, by S's buffer
   float lane_m[2][128], lane_l[2][2][128];  // a segment's maxima and (half) sums, per lane
   float q_scale[2][128];          // 2^-x of a query row's scaling (8-bit caches), per lane
@@ -407,6 +411,72 @@ __device__ __forceinline__ void softmax_tile(uint32_t lane_base, uint32_t s_at, 
   }
   l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
   tmem_store_wait();
+}
+
+// Which elements of a word of values are not finite, as a mask.
+template <bool F8>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  return F8 ? __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu) : __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u);
+}
+
+// A tile of values behind its first `by_all` tokens, which every row of the step
+// sees: the others meet weights of 0, and 0 * NaN is NaN.  Slots from `used` on
+// (beyond the request's length) hold anything and are zeroed; of the step's own
+// tokens, the values that are not finite (the rows that see them get them back on
+// their way out).  True: there were some in this thread's places.
+template <bool F8, int NBLK>
+__device__ __noinline__ bool clean_values(unsigned char* v, int by_all, int used, int tid) {
+  constexpr int TN = Cfg<F8, NBLK>::TN;
+  bool odd = false;
+#pragma unroll 1
+  for (int c = by_all * 8 + tid; c < TN * 8; c += 256)
+#pragma unroll
+    for (int b = 0; b < NBLK; ++b) {
+      uint4* to = reinterpret_cast<uint4*>(v + b * TN * 128 + c * 16);
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (c < used * 8) {
+        x = *to;
+        const uint4 out = make_uint4(not_finite<F8>(x.x), not_finite<F8>(x.y), not_finite<F8>(x.z), not_finite<F8>(x.w));
+        if (!(out.x | out.y | out.z | out.w)) continue;
+        odd = true;
+        x = make_uint4(x.x & ~out.x, x.y & ~out.y, x.z & ~out.z, x.w & ~out.w);
+      }
+      *to = x;
+    }
+  fence_proxy_async();
+  return odd;
+}
+
+// Adds to a segment's rows, in the output or in their part, the non-finite values of
+// the step's own tokens that they see, which clean_values has taken out of the tiles
+// (a positive weight times such a value is that value).  Out of line and after the
+// rows are out: few calls have such values, and what stands within the rows' way
+// out costs every call (a step over an 8-bit cache 164 us, with a branch there 176).
+template <bool F8, int NBLK>
+__device__ __noinline__ void add_not_finite(const Params& p, const Seg s, bool whole, long long part_row, int tid) {
+  using C = Cfg<F8, NBLK>;
+  const CacheView& c = p.a.c;
+  const int one_sees = s.len - s.n + 1, from = max(max(one_sees, 0), s.t0 * C::TN), to = min(s.len, s.t1 * C::TN);
+  for (int at = tid; at < s.rows * c.dim; at += 128) {
+    const int row = at / c.dim, d = at - row * c.dim, m = 128 * s.mt + row, j = row_of(p, m);
+    float x = 0.0f;
+    for (int t = from; t < min(to, one_sees + j); ++t) {
+      const int nth = t / c.page_size, page = __ldg(c.table + static_cast<long long>(s.i) * c.max_pages + nth);
+      if (page < 0 || page >= c.num_pages) continue;  // read as zeros
+      const long long el = slot_offset(c, page, t - nth * c.page_size) + s.kvh * c.head_stride + d;
+      const float v = F8 ? e4m3_to_float(__ldg(static_cast<const uint8_t*>(c.v) + el))
+                         : bf16_to_float(__ldg(static_cast<const uint16_t*>(c.v) + el));
+      if (!isfinite(v)) x += v;
+    }
+    if (isfinite(x)) continue;
+    if (whole) {
+      const int h = s.kvh * p.a.group + (m - j * p.a.group);
+      uint16_t* to_out = p.a.out + ((s.first + j) * static_cast<long long>(p.a.q_heads) + h) * c.dim + d;
+      *to_out = float_to_bf16(bf16_to_float(*to_out) + x);
+    } else {
+      p.part_o[(part_row + row) * C::DP + d] += x;
+    }
+  }
 }
 
 // Row of the workspace where part c of a segment that starts in CTA c0 begins.
@@ -895,6 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         rows_sync();
         base += W;
       }
+      if (sh.odd[segs & 3]) add_not_finite<F8, NBLK>(p, s, whole, part_row, L);
       if (!whole) {
         const long long G = min(static_cast<long long>(gridDim.x), sh.total);
         const auto cta_of = [&](long long x) { return static_cast<int>(((x + 1) * G - 1) / sh.total); };
@@ -935,6 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_empty[qb]);
       }
+      bool odd = false;
       for (int t = s.t0; t < s.t1; ++t, ++u) {
         const uint32_t buf = u & 1u;
         const uint32_t s_at = C::S_COL + buf * TN;
@@ -953,18 +1025,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             softmax_tile<F8, NBLK, TN / 2>(lane_base, s_at, first, copy, vis, sc, fresh, ref, l, buf, half, pv_done,
                                            pv_parity, sh, a.err);
         }
-        const int valid = s.len - t * TN;
-        if (valid < TN) {
-          // slots beyond the length hold anything, and 0 * NaN is NaN: zero
-          // the value rows (of the segment's last tile in the ring)
+        const int by_all = s.len - s.n + 1 - t * TN;  // tokens of the tile that every row of the step sees
+        if (by_all < TN) {
           Ring<C::NS> vt = at;
-          vt.skip(2 * (s.t1 - s.t0) - 1);
+          vt.skip(2 * (t - s.t0) + 1);
           wait_or_stop(&sh.kv_full[vt.slot], vt.turn, sh, a.err);
-          unsigned char* v = ring + vt.slot * C::SLOT;
-          for (int c = max(valid, 0) * 8 + tid; c < TN * 8; c += 256)
-#pragma unroll
-            for (int b = 0; b < NBLK; ++b) *reinterpret_cast<uint4*>(v + b * TN * 128 + c * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async();
+          odd |= clean_values<F8, NBLK>(ring + vt.slot * C::SLOT, max(by_all, 0), s.len - t * TN, tid);
         }
         tc_fence_before();
         __syncwarp();
@@ -975,6 +1041,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (segs >= 2) wait_or_stop(&sh.sums_empty[sb], ((segs >> 1) - 1) & 1, sh, a.err);
       if (half == 0) sh.lane_m[sb][L] = ref == -INFINITY ? -INFINITY : ref * sc - C::LIFT;
       sh.lane_l[sb][half][L] = l;
+      odd = __any_sync(kFull, odd);
+      if (lane == 0) reinterpret_cast<unsigned char*>(&sh.odd[segs & 3])[warp] = odd;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.sums_full[sb]);
       ++segs;

@@ -1,0 +1,98 @@
+"""sd_cache_append and sd_attend at values, scales and lengths that are out of the ordinary.
+
+Tolerances are those of test_gpu_cache_attend.py.
+"""
+import pytest
+
+import serving_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import speculative_decoding_verification_sd_gb300 as sd  # noqa: E402
+from test_gpu_cache_attend import compare, device_cache  # noqa: E402
+
+i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+NAN, INF = float("nan"), float("inf")
+
+
+def attend_with(counts, lens, heads, group, dim, page, e4m3, spoil, seed=0):
+    """A step over a cache in which `spoil(k, v, at)` has set elements; at(i, t) = (page, slot)."""
+    g = torch.Generator().manual_seed(seed)
+    k_max = max(counts) - 1
+    k, v, table, ks, vs = ref.make_cache(g, lens, page, heads, dim, e4m3)
+    spoil(k, v, lambda i, t: (int(table[i, t // page]), t % page))
+    cu = ref.compaction(counts)
+    used = int(cu[-1])
+    q = torch.randn((len(counts) * (k_max + 1), heads * group, dim), generator=g).bfloat16()
+    cache = device_cache(k, v, table, ks, vs)
+    r = sd.attend(q.cuda(), cache, torch.tensor(cu).cuda(), i32(lens), k_max, lse=True)
+    torch.cuda.synchronize()
+    assert int(r.err) == 0
+    want, wlse, mass = ref.attend(q[:used], k, v, table, ks, vs, cu, lens, dim ** -0.5)
+    out, lse = r.out.cpu()[:used].double(), r.lse.cpu()[:used].double()
+    # where the definition is not finite, the same value; elsewhere within the usual bound
+    odd = ~torch.isfinite(want)
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert torch.equal(torch.where(odd, out, 0.0).nan_to_num(nan=0.0), torch.where(odd, want, 0.0).nan_to_num(nan=0.0))
+    assert torch.equal(torch.isnan(lse), torch.isnan(wlse))
+    only = lambda x: torch.where(odd, 0.0, x)  # noqa: E731
+    alive = lambda x: torch.where(torch.isnan(wlse), 0.0, x)  # noqa: E731
+    compare(q[:used], k, ks, dim ** -0.5, only(out), alive(lse), only(want), alive(wlse), only(mass))
+    return out, want
+
+
+# a step of four whose own tokens lie in one tile, across two, at the start, and far down a split cache
+STEPS = [([4, 1, 3], [100, 50, 3]), ([4, 16, 2], [130, 260, 129]), ([16], [16]), ([5], [30000]), ([5], [29954]), ([8], [129])]
+
+
+@pytest.mark.parametrize("page", [16, 5])
+@pytest.mark.parametrize("dim,heads,group", [(64, 2, 4), (128, 1, 16), (256, 1, 2), (80, 3, 1)])
+@pytest.mark.parametrize("counts,lens", STEPS)
+def test_a_value_reaches_no_row_that_does_not_see_it(counts, lens, dim, heads, group, page):
+    """The last token's values, and those of one in the middle of the step, are not finite
+    in some columns: rows before them are as without, rows from them on get the
+    definition's infinity or NaN there, and their other columns are untouched."""
+    for e4m3 in (False, True):
+        def spoil(k, v, at):
+            for i, (n, L) in enumerate(zip(counts, lens)):
+                if n < 2:
+                    continue
+                last, mid = at(i, L - 1), at(i, L - n // 2 - 1)
+                v[last][0, 3] = NAN if e4m3 else INF
+                v[last][0, dim - 1] = NAN
+                if not e4m3:
+                    v[last][0, 5] = -INF
+                    if n > 2:
+                        v[mid][0, 5], v[mid][0, 6] = INF, -INF
+        out, want = attend_with(counts, lens, heads, group, dim, page, e4m3, spoil)
+        assert bool(torch.isfinite(out[0]).all())
+        assert not bool(torch.isfinite(want).all())
+
+
+@pytest.mark.parametrize("page", [16, 5])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_step_of_values_that_are_all_nan(page, e4m3):
+    """Every row of the step carries NaN values: the first sees its own, so all are NaN;
+    with the first one sound, it alone is finite."""
+    for whole in (True, False):
+        def spoil(k, v, at):
+            for t in range(0 if whole else 1, 6):
+                v[at(0, 194 + t)] = NAN
+        out, _ = attend_with([6], [200], 2, 8, 128, page, e4m3, spoil)
+        assert bool(torch.isnan(out[1:]).all()) and bool(torch.isnan(out[0]).all()) == whole
+
+
+@pytest.mark.parametrize("page", [16, 5])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_key_reaches_no_row_that_does_not_see_it(page, e4m3):
+    for counts, lens in STEPS:
+        def spoil(k, v, at):
+            for i, (n, L) in enumerate(zip(counts, lens)):
+                if n > 1:
+                    k[at(i, L - 1)][0, 2] = NAN
+        out, _ = attend_with(counts, lens, 2, 4, 128, page, e4m3, spoil)
+        assert bool(torch.isfinite(out[0]).all())
