@@ -40,9 +40,10 @@
 // 8-bit caches feed the tensor core as they are.  A query (8 significant
 // bits) is the sum of two e4m3 terms after scaling its row by a power of two,
 // exact but for elements below 2^-13 of the row's largest (off by up to 2^-17 of
-// it); P is rounded to 9 significant bits and split into three e5m2 terms
-// (e5m2 is the upper byte of a half), whose exponents reach 2^-27 of the
-// largest weight, so a long tail of small weights is not lost.  The products
+// it); P becomes a half, which is split into three e5m2 terms (e5m2 is the upper
+// byte of a half), the last one to nearest: within 2^-9 of a weight at worst and
+// 2^-11 at the root mean square, and their exponents reach 2^-27 of the largest
+// weight, so a long tail of small weights is not lost.  The products
 // of the terms accumulate in the same fp32 accumulators.
 //
 // What bounds it.  The cache's bytes over a bf16 cache: 19 requests of 65536
@@ -385,11 +386,13 @@ __device__ __forceinline__ void softmax_tile(uint32_t lane_base, uint32_t s_at, 
           sum[2 * e] += x;
           sum[2 * e + 1] += y;
           asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hf[e]) : "f"(y), "f"(x));
-          hf[e] += 0x00020002u;  // to nearest at 9 bits; the split below drops the rest
         }
 #pragma unroll
         for (int t = 0; t < C::PPARTS; ++t) {
-          w[t][c] = __byte_perm(hf[0], hf[1], 0x7531);  // the upper bytes
+          // the upper bytes; the last ones to nearest (rounding before the split would
+          // add half a step to every weight whose terms hold it in full)
+          const uint32_t near = t == C::PPARTS - 1 ? 0x00800080u : 0u;
+          w[t][c] = __byte_perm(hf[0] + near, hf[1] + near, 0x7531);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const uint32_t top = hf[e] & 0xFF00FF00u;

@@ -96,3 +96,23 @@ def test_a_key_reaches_no_row_that_does_not_see_it(page, e4m3):
                     k[at(i, L - 1)][0, 2] = NAN
         out, _ = attend_with(counts, lens, 2, 4, 128, page, e4m3, spoil)
         assert bool(torch.isfinite(out[0]).all())
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("page", [16, 5])
+def test_equal_weights_give_the_mean(page, e4m3):
+    """Queries of zeros: every weight is the same power of two and exact in any format,
+    so what is left are the fp32 sums (2^-24 a token) and the output's own rounding,
+    half a bf16 step of that value.  One token alone gives its own values."""
+    g = torch.Generator().manual_seed(7)
+    lens, counts = [1, 3, 100, 700, 16], [1, 2, 1, 4, 16]
+    k, v, table, ks, vs = ref.make_cache(g, lens, page, 2, 128, e4m3)
+    cu = ref.compaction(counts)
+    used = int(cu[-1])
+    q = torch.zeros((5 * 16, 8, 128), dtype=torch.bfloat16)
+    r = sd.attend(q.cuda(), device_cache(k, v, table, ks, vs), torch.tensor(cu).cuda(), i32(lens), 15)
+    torch.cuda.synchronize()
+    want, _, mass = ref.attend(q[:used], k, v, table, ks, vs, cu, lens, 128 ** -0.5)
+    step = torch.exp2(torch.floor(torch.log2(want.abs().clamp(min=1e-30))) - 7)
+    off = (r.out.cpu()[:used].double() - want).abs()
+    assert bool((off <= step / 2 * (1 + 2.0 ** -10) + 700 * 2.0 ** -24 * mass).all()), float((off / step).max())
