@@ -13,7 +13,7 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 import speculative_decoding_verification_sd_gb300 as sd  # noqa: E402
-from test_gpu_cache_attend import compare, device_cache  # noqa: E402
+from test_gpu_cache_attend import compare, device_cache, run_attend  # noqa: E402
 
 i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
 NAN, INF = float("nan"), float("inf")
@@ -116,3 +116,33 @@ def test_equal_weights_give_the_mean(page, e4m3):
     step = torch.exp2(torch.floor(torch.log2(want.abs().clamp(min=1e-30))) - 7)
     off = (r.out.cpu()[:used].double() - want).abs()
     assert bool((off <= step / 2 * (1 + 2.0 ** -10) + 700 * 2.0 ** -24 * mass).all()), float((off / step).max())
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("page", [16, 5])
+def test_weights_keep_more_bits_than_the_output(page, e4m3):
+    """Half a bf16 step of the output; of the weights 2^-16 + 2^-18 (two bf16 terms) or
+    2^-9 + 2^-11 (a half in three e5m2 terms) and 2^-21 of the exponential; the logits'
+    and the sums' fp32 roundings as elsewhere."""
+    lens = [2, 3, 5, 9, 20, 130, 700]
+    s = run_attend([2] * 7, lens, 2, 4, 128, page, e4m3, seed=11, sharp=1.5)
+    k, v, table = s["cache"].k.cpu(), s["cache"].v.cpu(), s["cache"].page_table.cpu()
+    ks, vs = (None if x is None else x.cpu() for x in (s["cache"].k_scale, s["cache"].v_scale))
+    q = s["q"].cpu()
+    want, _, mass = ref.attend(q, k, v, table, ks, vs, s["cu"].cpu(), lens, s["scale"])
+    kmax = float(k.float().abs().max()) * (float(ks.max()) if e4m3 else 1.0)
+    logit = (128 + 4) * 2.0 ** -24 * q.double().abs().sum(-1)[..., None] * kmax * s["scale"]
+    step = torch.exp2(torch.floor(torch.log2(want.abs().clamp(min=1e-30))) - 7)
+    weight = (2.0 ** -9 + 2.0 ** -11 if e4m3 else 2.0 ** -16 + 2.0 ** -18) + 2.0 ** -21 + 700 * 2.0 ** -24 + 2 * logit
+    off = (s["out"].cpu().double() - want).abs()
+    assert bool((off <= step / 2 * (1 + 2.0 ** -10) + weight * mass).all()), float((off - weight * mass).div(step).max())
+
+
+@pytest.mark.parametrize("page", [16, 5])
+def test_an_infinite_value_that_all_rows_see(page):
+    def spoil(k, v, at):
+        v[at(0, 0)][0, 3], v[at(0, 0)][0, 4] = INF, -INF
+        v[at(1, 20)][1, 0], v[at(1, 40)][1, 0] = INF, -INF
+    out, want = attend_with([3, 4], [300, 129], 2, 4, 64, page, False, spoil)
+    assert bool((out[:3, :4, 3] == INF).all()) and bool((out[:3, :4, 4] == -INF).all())
+    assert bool(torch.isnan(out[3:, 4:, 0]).all()) and int((~torch.isfinite(out)).sum()) == 3 * 4 * 2 + 4 * 4
