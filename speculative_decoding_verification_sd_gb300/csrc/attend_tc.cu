@@ -1008,7 +1008,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int m = 128 * s.mt + min(r, s.rows - 1), j = row_of(p, m);
       const int seen = s.len - s.n + j + 1;
       const bool busy = (L & 96) % R < s.rows;  // this warp holds rows
-      float sc = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
+      float sc = fabsf(a.scale) * kLog2e;
       if (F8) {
         const uint32_t qb = segs % C::NQ;
         wait_or_stop(&sh.q_full[qb], (segs / C::NQ) & 1, sh, a.err);
@@ -1017,6 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_empty[qb]);
       }
+      sc = sc < 1e-37f ? 1e-37f : sc;  // masked scores are -inf, and -inf * 0 is NaN
       bool odd = false;
       for (int t = s.t0; t < s.t1; ++t, ++u) {
         const uint32_t buf = u & 1u;

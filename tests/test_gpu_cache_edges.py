@@ -146,3 +146,22 @@ def test_an_infinite_value_that_all_rows_see(page):
     out, want = attend_with([3, 4], [300, 129], 2, 4, 64, page, False, spoil)
     assert bool((out[:3, :4, 3] == INF).all()) and bool((out[:3, :4, 4] == -INF).all())
     assert bool(torch.isnan(out[3:, 4:, 0]).all()) and int((~torch.isfinite(out)).sum()) == 3 * 4 * 2 + 4 * 4
+
+
+@pytest.mark.parametrize("page", [16, 5])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("scale", [0.0, 1e-8, 0.09])
+def test_queries_near_the_smallest_normal(scale, e4m3, page):
+    """Logits of next to nothing: every visible token weighs the same."""
+    g = torch.Generator().manual_seed(4)
+    lens, counts = [200, 3], [2, 3]
+    k, v, table, ks, vs = ref.make_cache(g, lens, page, 1, 64, e4m3)
+    if e4m3:
+        ks = torch.full_like(ks, 1e-4)
+    for size in (2.0 ** -126, 2.0 ** -133, 2.0 ** -110):
+        q = torch.full((6, 4, 64), size).bfloat16()
+        cache = device_cache(k, v, table, ks, vs)
+        r = sd.attend(q.cuda(), cache, torch.tensor(ref.compaction(counts)).cuda(), i32(lens), 2, scale=scale, lse=True)
+        torch.cuda.synchronize()
+        want, wlse, mass = ref.attend(q[:5], k, v, table, ks, vs, ref.compaction(counts), lens, scale)
+        compare(q[:5], k, ks, scale, r.out.cpu()[:5], r.lse.cpu()[:5], want, wlse, mass)
