@@ -372,6 +372,7 @@ sd_status sd_calibrate_apply(const float* conf_logits, const int* draft_lens, in
  *              NULL for SD_BF16.  Scales are finite and > 0 (not checked).
  * Limits: heads >= 1, 8 <= head_dim <= SD_MAX_HEAD_DIM and a multiple of 8. */
 #define SD_MAX_HEAD_DIM 256
+#define SD_MAX_LEN 0x7FFFFC00 /* tokens that sd_attend reads of a request at most */
 typedef struct {
   void* k;
   void* v;
@@ -421,7 +422,8 @@ sd_status sd_cache_append(const void* k_new, const void* v_new, long long row_st
  *   lse_out    [rows, q_heads] fp32 (natural logarithm) or NULL.
  *   err_flag   SD_DEV_ERR_CU_SEQLENS: a request's row range is invalid (its
  *              rows are not written); SD_DEV_ERR_CACHE: kv_lens[i] outside
- *              [0, max_pages * page_size] (clamped into it), or a page id
+ *              [0, max_pages * page_size] or above SD_MAX_LEN (clamped into
+ *              the range), or a page id
  *              outside [0, num_pages) (its keys and values read as zeros).
  *   workspace  sd_attend_workspace_bytes(...) bytes, 256-byte aligned,
  *              zero-filled once before its first use; every call leaves its

@@ -32,7 +32,7 @@ from ._lib import (SD_NOALLOC_SCRATCH_BYTES, SD_BF16, SD_DEV_ERR_CACHE, SD_DEV_E
                    SD_DEV_ERR_DRAFT_ID, SD_DEV_ERR_DRAFT_LENS, SD_DEV_ERR_LOGITS, SD_DEV_ERR_OUTCOME,
                    SD_DEV_ERR_TEMP, SD_DEV_ERR_TIMEOUT, SD_DEV_ERR_TRUNC, SD_DEV_ERR_UNIFORM, SD_E4M3, SD_ERR_CUDA,
                    SD_ERR_DEVICE_CHECK, SD_ERR_INVALID_ARG, SD_ERR_SHAPE, SD_ERR_UNSUPPORTED,
-                   SD_F32, SD_MAX_HEAD_DIM, SD_MAX_HEAD_GROUP, SD_MAX_K, SD_MAX_PLAN_SLOTS, SD_MAX_ROW_BYTES, SD_MAX_SAMPLE_ROW_BYTES, SD_MAX_V, SD_MAX_VERIFY_BS,
+                   SD_F32, SD_MAX_HEAD_DIM, SD_MAX_HEAD_GROUP, SD_MAX_K, SD_MAX_LEN, SD_MAX_PLAN_SLOTS, SD_MAX_ROW_BYTES, SD_MAX_SAMPLE_ROW_BYTES, SD_MAX_V, SD_MAX_VERIFY_BS,
                    SD_MODE_ADAPTIVE, SD_MODE_ALL_SLOTS, SD_MODE_UNIFORM_K, SD_OK,
                    SD_VERIFY_DRAFT_PADDED, SD_VERIFY_EARLY_EXIT, SD_VERIFY_TEST_STALL, SdError,
                    sd_kv_cache, sd_launch_cfg)

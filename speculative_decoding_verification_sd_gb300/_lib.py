@@ -37,6 +37,7 @@ SD_MAX_VERIFY_BS = 4096
 SD_MAX_V = 1 << 20
 SD_MAX_ROW_BYTES = 2 << 20
 SD_MAX_HEAD_DIM = 256
+SD_MAX_LEN = 0x7FFFFC00
 SD_MAX_HEAD_GROUP = 128
 SD_MAX_SAMPLE_ROW_BYTES = 3 << 19
 

@@ -31,9 +31,7 @@ __global__ void __launch_bounds__(32 * kWarps) attend_rows_kernel(const AttendPa
   const int R = p.k_max + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = blockIdx.x / R, j = blockIdx.x - i * R, h = blockIdx.y, kvh = h / p.group;
   const RowRange r = row_range(p.cu, i, p.bs, p.k_max);
-  const int room = static_cast<int>(
-      min(static_cast<long long>(p.c.max_pages) * p.c.page_size, 0x7fffffffLL));
-  const int given = __ldg(p.lens + i), len = min(max(given, 0), room);
+  const int given = __ldg(p.lens + i), len = attended_len(p.c, given);
   if (threadIdx.x == 0 && j == 0 && h == 0) {
     if (r.n < 0) raise_error(p.err, SD_DEV_ERR_CU_SEQLENS);
     if (given != len) raise_error(p.err, SD_DEV_ERR_CACHE);

@@ -162,12 +162,10 @@ struct Walk {
   // Units of request i (0: no rows, or an invalid range).
   __device__ static long long units(const AttendParams& p, int i, Seg& s, int& mts) {
     const RowRange r = row_range(p.cu, i, p.bs, p.k_max);
-    const long long room = static_cast<long long>(p.c.max_pages) * p.c.page_size;
-    const int given = __ldg(p.lens + i);
     s.i = i;
     s.first = r.first;
     s.n = r.n;
-    s.len = static_cast<int>(min(static_cast<long long>(max(given, 0)), room));
+    s.len = attended_len(p.c, __ldg(p.lens + i));
     s.tiles = max(1, (s.len + TN - 1) / TN);
     mts = r.n > 0 ? (r.n * p.group + 127) / 128 : 0;
     return static_cast<long long>(p.c.heads) * mts * (s.tiles + LEAD);

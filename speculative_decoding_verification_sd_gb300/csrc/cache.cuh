@@ -23,6 +23,13 @@ __device__ __forceinline__ RowRange row_range(const int* cu, int i, int bs, int 
   return ok ? RowRange{a, b - a} : RowRange{0, -1};
 }
 
+// A request's length as attention takes it.  Kernels step past the last token by up
+// to a tile, so lengths stop short of 2^31.
+__device__ __forceinline__ int attended_len(const CacheView& c, int given) {
+  const long long room = static_cast<long long>(c.max_pages) * c.page_size;
+  return min(max(given, 0), static_cast<int>(min(room, static_cast<long long>(SD_MAX_LEN))));
+}
+
 // Element offset of (page, slot) in the cache tensors.
 __device__ __forceinline__ long long slot_offset(const CacheView& c, int page, int slot) {
   return page * c.page_stride + slot * c.token_stride;

@@ -2,6 +2,8 @@
 
 Tolerances are those of test_gpu_cache_attend.py.
 """
+import math
+
 import pytest
 
 import serving_reference as ref
@@ -165,3 +167,17 @@ def test_queries_near_the_smallest_normal(scale, e4m3, page):
         torch.cuda.synchronize()
         want, wlse, mass = ref.attend(q[:5], k, v, table, ks, vs, ref.compaction(counts), lens, scale)
         compare(q[:5], k, ks, scale, r.out.cpu()[:5], r.lse.cpu()[:5], want, wlse, mass)
+
+
+def test_lengths_next_to_2_to_the_31():
+    """One page of 65536 tokens named 32768 times: keys of 0 and values of 1 give
+    1 and the logarithm of the length, and longer lengths are cut with their bit."""
+    page, most = 65536, sd.SD_MAX_LEN
+    k, v = (torch.full((1, page, 1, 8), x, dtype=torch.bfloat16, device="cuda") for x in (0.0, 1.0))
+    cache = sd.KVCache(k, v, torch.zeros((1, 2 ** 31 // page), dtype=torch.int32, device="cuda"))
+    q = torch.ones((1, 1, 8), dtype=torch.bfloat16, device="cuda")
+    for length, bit in ((most, 0), (2 ** 31 - 1, sd.SD_DEV_ERR_CACHE)):
+        r = sd.attend(q, cache, i32([0, 1]), i32([length]), 0, lse=True)
+        torch.cuda.synchronize()
+        assert int(r.err) == bit and bool((r.out == 1).all())
+        assert abs(float(r.lse) - math.log(most)) <= 8 * 2.0 ** -22 + 2.0 ** -23 * math.log(most)
