@@ -181,3 +181,70 @@ def test_lengths_next_to_2_to_the_31():
         torch.cuda.synchronize()
         assert int(r.err) == bit and bool((r.out == 1).all())
         assert abs(float(r.lse) - math.log(most)) <= 8 * 2.0 ** -22 + 2.0 ** -23 * math.log(most)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("dim", [136, 160, 192, 72, 248])
+def test_head_dims_that_leave_a_column_block_empty(dim, e4m3):
+    run_attend([4, 1, 3, 16], [100, 1, 3, 333], 2, 3, dim, 16, e4m3, seed=dim)
+
+
+@pytest.mark.parametrize("page", [16, 5])
+def test_bad_pages_and_lengths_over_an_8_bit_cache(page):
+    s = run_attend([1, 2], [40, 60], 2, 2, 64, page, True, k_max=1)
+    call = lambda cu=None, lens=None: sd.attend(s["q"], s["cache"], s["cu"] if cu is None else cu,  # noqa: E731
+                                                s["lens"] if lens is None else lens, 1, workspace=s["ws"])
+    table = s["cache"].page_table
+    for bad in (-1, 10 ** 6, s["cache"].num_pages):
+        keep = table[1, 1].clone()
+        table[1, 1] = bad
+        r = call()
+        torch.cuda.synchronize()
+        assert int(r.err) == sd.SD_DEV_ERR_CACHE
+        assert torch.equal(r.out[0], s["out"][0]) and bool(torch.isfinite(r.out).all())
+        table[1, 1] = keep
+    for length in (-1, 10 ** 9):
+        r = call(lens=i32([40, length]))
+        torch.cuda.synchronize()
+        assert int(r.err) & sd.SD_DEV_ERR_CACHE and torch.equal(r.out[0], s["out"][0])
+    for cu in ([0, 3, 4], [0, 1, 0], [-1, 1, 2], [0, 1, 5]):
+        r = call(cu=i32(cu))
+        torch.cuda.synchronize()
+        assert int(r.err) == sd.SD_DEV_ERR_CU_SEQLENS
+    r = call()
+    torch.cuda.synchronize()
+    assert int(r.err) == 0 and torch.equal(r.out[:3], s["out"][:3])
+
+
+@pytest.mark.parametrize("off", [0, 1])
+def test_append_quotients_far_from_one(off):
+    """Scales around and beyond 1e-18 and 1e18 and elements around and beyond 2^59: the
+    fp32 quotient, rounded to e4m3, bit for bit."""
+    scales = torch.tensor([1e-18, 1.0000001e-18, 9.99e-19, 1e-30, 3e-39, 1e18, 9.9999997e17, 1.01e18, 1e30, 3e38, 0.02, 1.0])
+    x = torch.tensor([2.0 ** 59, 2.0 ** 59 * 0.99609375, 2.0 ** 60, 3e38, 1e-38, 1e-40, 0.0, -1.0, -(2.0 ** 59), 447.0,
+                      1e-18, -3e-17, 2e18, 4.4e20, -1e9, 0.019])
+    heads, dim = len(scales), 16
+    new = x.bfloat16().view(1, 1, dim).expand(1, heads, dim).contiguous()
+    k, v = (torch.zeros((1, 4 * heads * dim + off), dtype=torch.uint8, device="cuda")[:, off:]
+            .view(torch.float8_e4m3fn).unflatten(1, (4, heads, dim)) for _ in range(2))
+    cache = sd.KVCache(k, v, i32([[0]]), k_scale=scales.cuda(), v_scale=scales.cuda())
+    err = sd.append(new.cuda(), new.cuda(), cache, i32([0, 1]), i32([3]), 0)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    want = (new[0].float() / scales[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    for got in (k, v):
+        assert torch.equal(got[0, 2].view(torch.uint8).cpu(), want)
+        assert not got[0, [0, 1, 3]].view(torch.uint8).any()
+
+
+def test_sample_leaves_every_row_of_an_invalid_range_alone():
+    z = torch.randn((8, 512), generator=torch.Generator().manual_seed(4)).cuda()
+    for cu in ([0, -2], [5, 3], [0, 9], [4, 2, 3]):
+        kept = torch.full_like(z, 77.0)
+        tokens = torch.full((8,), -5, dtype=torch.int32, device="cuda")
+        r = sd.sample(z, torch.ones(2).cuda(), torch.full((8,), 0.5).cuda(), tokens=tokens, kept=kept, cu_seqlens=i32(cu))
+        torch.cuda.synchronize()
+        assert int(r.err) == sd.SD_DEV_ERR_CU_SEQLENS
+        live = [2] if cu == [4, 2, 3] else []
+        rest = [row for row in range(8) if row not in live]
+        assert bool((kept[rest] == 77.0).all()) and bool((tokens[rest] == -5).all())
