@@ -667,7 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     Seg s;
     const auto load = [&](const CUtensorMap* map, const int (&c)[4], bool in, int bytes) {
       if (turned) wait_or_stop(&sh.kv_empty[at.slot], at.turn ^ 1, sh, a.err);
-      if (*static_cast<volatile int*>(&sh.stop)) return;
+      // (the whole warp or none of it: the lanes meet below)
+      if (__any_sync(kFull, *static_cast<volatile int*>(&sh.stop))) return;
       if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[at.slot], bytes);
       __syncwarp();
       if (in)
