@@ -443,6 +443,17 @@ sd_status sd_attend(const void* q, long long q_row_stride, int q_heads, const sd
                     void* out, float* lse_out, int* err_flag, void* workspace, size_t ws_bytes,
                     void* stream);
 
+/* sd_attend and sd_sample (below) with options: cfg may be NULL; of its fields
+ * wait_limit_us holds as for sd_verify_ex, flags may be SD_TEST_STALL, the rest
+ * has to be 0. */
+#define SD_TEST_STALL 0x100 /* test hook: nothing is loaded, so the waits for it run out (after
+                               wait_limit_us) and the time-out path runs; kernels that wait
+                               for no copy (caches of any layout, rows off 16 bytes) ignore it */
+sd_status sd_attend_ex(const void* q, long long q_row_stride, int q_heads,
+                       const sd_kv_cache* cache, const int* cu_seqlens, const int* kv_lens, int bs,
+                       int k_max, float scale, void* out, float* lse_out, int* err_flag,
+                       void* workspace, size_t ws_bytes, const sd_launch_cfg* cfg, void* stream);
+
 /* sd_sample -- sampling with temperature, top-k, top-p and min-p from given
  * uniforms, and the truncated rows themselves.  For a row z at temperature
  * tau > 0, with m = max z and w_l = exp((z_l - m) / tau), tokens ordered by (z
@@ -489,6 +500,10 @@ sd_status sd_sample(const void* logits, sd_dtype dt, int V, int rows, const int*
                     const float* temps, const int* top_k, const float* top_p, const float* min_p,
                     const float* uniforms, int* tokens, void* kept_out, int* err_flag,
                     void* stream);
+sd_status sd_sample_ex(const void* logits, sd_dtype dt, int V, int rows, const int* cu_seqlens,
+                       int bs, const float* temps, const int* top_k, const float* top_p,
+                       const float* min_p, const float* uniforms, int* tokens, void* kept_out,
+                       int* err_flag, const sd_launch_cfg* cfg, void* stream);
 
 const char* sd_status_string(sd_status s);
 

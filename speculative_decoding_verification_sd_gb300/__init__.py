@@ -34,13 +34,13 @@ from ._lib import (SD_NOALLOC_SCRATCH_BYTES, SD_BF16, SD_DEV_ERR_CACHE, SD_DEV_E
                    SD_ERR_DEVICE_CHECK, SD_ERR_INVALID_ARG, SD_ERR_SHAPE, SD_ERR_UNSUPPORTED,
                    SD_F32, SD_MAX_HEAD_DIM, SD_MAX_HEAD_GROUP, SD_MAX_K, SD_MAX_LEN, SD_MAX_PLAN_SLOTS, SD_MAX_ROW_BYTES, SD_MAX_SAMPLE_ROW_BYTES, SD_MAX_V, SD_MAX_VERIFY_BS,
                    SD_MODE_ADAPTIVE, SD_MODE_ALL_SLOTS, SD_MODE_UNIFORM_K, SD_OK,
-                   SD_VERIFY_DRAFT_PADDED, SD_VERIFY_EARLY_EXIT, SD_VERIFY_TEST_STALL, SdError,
+                   SD_TEST_STALL, SD_VERIFY_DRAFT_PADDED, SD_VERIFY_EARLY_EXIT, SD_VERIFY_TEST_STALL, SdError,
                    sd_kv_cache, sd_launch_cfg)
 
 __all__ = [
     "sd_plan", "sd_verify", "sd_verify_ex", "sd_verify_noalloc", "sd_plan_workspace_bytes",
     "sd_verify_workspace_bytes", "sd_verify_launch_info", "sd_calibrate", "sd_calibrate_apply",
-    "sd_cache_append", "sd_attend_workspace_bytes", "sd_attend", "sd_sample",
+    "sd_cache_append", "sd_attend_workspace_bytes", "sd_attend", "sd_attend_ex", "sd_sample", "sd_sample_ex",
     "plan", "verify", "append", "attend", "sample", "attend_workspace", "KVCache", "PlanResult",
     "VerifyResult", "AttendResult", "SampleResult", "SdError", "build", "library_path", "verify_workspace",
 ]
@@ -364,6 +364,25 @@ def sd_sample(logits, dt, V, rows, cu_seqlens, bs, temps, top_k, top_p, min_p, u
                                _ptr(temps), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(uniforms),
                                _ptr(tokens), _ptr(kept_out), _ptr(err_flag), _stream(stream))
     return _lib.check("sd_sample", st)
+
+
+def sd_attend_ex(q, q_row_stride, q_heads, cache, cu_seqlens, kv_lens, bs, k_max, scale, out,
+                 lse_out, err_flag, workspace, ws_bytes, cfg=None, stream=None):
+    st = _lib.load().sd_attend_ex(q if isinstance(q, int) else q.data_ptr(), int(q_row_stride),
+                                  int(q_heads), _cache(cache), _ptr(cu_seqlens), _ptr(kv_lens),
+                                  int(bs), int(k_max), float(scale), _ptr(out), _ptr(lse_out),
+                                  _ptr(err_flag), _ptr(workspace), int(ws_bytes), _cfg(cfg),
+                                  _stream(stream))
+    return _lib.check("sd_attend_ex", st)
+
+
+def sd_sample_ex(logits, dt, V, rows, cu_seqlens, bs, temps, top_k, top_p, min_p, uniforms, tokens,
+                 kept_out, err_flag, cfg=None, stream=None):
+    st = _lib.load().sd_sample_ex(_ptr(logits), _dt(dt), int(V), int(rows), _ptr(cu_seqlens),
+                                  int(bs), _ptr(temps), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+                                  _ptr(uniforms), _ptr(tokens), _ptr(kept_out), _ptr(err_flag),
+                                  _cfg(cfg), _stream(stream))
+    return _lib.check("sd_sample_ex", st)
 
 
 def attend_workspace(bs: int, k_max: int, q_heads: int, cache: KVCache, device=None) -> torch.Tensor:

@@ -44,12 +44,13 @@ SD_MAX_SAMPLE_ROW_BYTES = 3 << 19
 SD_VERIFY_EARLY_EXIT = 0x1
 SD_VERIFY_DRAFT_PADDED = 0x2
 SD_VERIFY_TEST_STALL = 0x100
+SD_TEST_STALL = 0x100
 
 # Every symbol include/sd.h declares.
 EXPORTS = ("sd_plan_workspace_bytes", "sd_plan", "sd_verify_workspace_bytes", "sd_verify",
            "sd_verify_ex", "sd_verify_noalloc", "sd_verify_launch_info", "sd_calibrate",
            "sd_calibrate_apply", "sd_cache_append", "sd_attend_workspace_bytes", "sd_attend",
-           "sd_sample", "sd_status_string", "sd_last_error_string", "sd_abi_version")
+           "sd_attend_ex", "sd_sample", "sd_sample_ex", "sd_status_string", "sd_last_error_string", "sd_abi_version")
 SD_NOALLOC_SCRATCH_BYTES = 16 << 20  # include/sd.h
 
 
@@ -123,8 +124,12 @@ def load(path: Path | None = None) -> ctypes.CDLL:
     lib.sd_attend_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
     lib.sd_attend.restype = i32
     lib.sd_attend.argtypes = [P, i64, i32, cache, P, P, i32, i32, f32, P, P, P, P, sz, P]
+    lib.sd_attend_ex.restype = i32
+    lib.sd_attend_ex.argtypes = lib.sd_attend.argtypes[:-1] + [ctypes.POINTER(sd_launch_cfg), P]
     lib.sd_sample.restype = i32
     lib.sd_sample.argtypes = [P, i32, i32, i32, P, i32, P, P, P, P, P, P, P, P, P]
+    lib.sd_sample_ex.restype = i32
+    lib.sd_sample_ex.argtypes = lib.sd_sample.argtypes[:-1] + [ctypes.POINTER(sd_launch_cfg), P]
     _lib = lib
     return lib
 

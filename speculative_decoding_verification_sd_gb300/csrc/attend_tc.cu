@@ -107,6 +107,10 @@ struct Cfg {
   static_assert(Q_COL + NQ * QC <= 512 && NS >= 3);
 };
 
+struct Wait {
+  int stop;  // a wait gave up
+  uint32_t limit_us;
+};
 struct Shared {
   uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots];
   // per buffer of S: scores there, weights there, weights used (a waiter is
@@ -116,7 +120,7 @@ struct Shared {
   uint64_t sums_full[2], sums_empty[2];  // per buffer of the softmax's final maxima and sums
   uint64_t o_free, end, end2;
   uint32_t tmem;
-  int stop;                       // a wait gave up
+  Wait wait;
   int start_i;                    // first request of this CTA's share ...
   long long start_off, u0, u1, total;  // ... and the unit within it; the share; all units
   int last;                       // this CTA joins a segment's parts
@@ -244,19 +248,19 @@ __device__ __forceinline__ int copies(int rows) { return F8 && rows <= 64 ? 2 : 
 // A wait that gives up when its time is over or another wait of the CTA gave
 // up; after that no wait of the CTA waits.  Out of line: see what bounds the
 // kernel.
-__device__ __noinline__ void wait_long(uint64_t* bar, uint32_t parity, volatile int* stop, int* err) {
-  const uint64_t end = clock_ns() + kWaitNs;
+__device__ __noinline__ void wait_long(uint64_t* bar, uint32_t parity, volatile Wait* wait, int* err) {
+  const uint64_t end = clock_ns() + wait->limit_us * 1000ull;
   while (!phase_done(bar, parity)) {
-    if (*stop) return;
+    if (wait->stop) return;
     if (clock_ns() > end) {
-      *stop = 1;
+      wait->stop = 1;
       raise_error(err, SD_DEV_ERR_TIMEOUT);
       return;
     }
   }
 }
 __device__ __forceinline__ void wait_or_stop(uint64_t* bar, uint32_t parity, Shared& sh, int* err) {
-  if (!phase_done(bar, parity)) wait_long(bar, parity, &sh.stop, err);
+  if (!phase_done(bar, parity)) wait_long(bar, parity, &sh.wait, err);
 }
 
 __device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -604,7 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.o_free, 4);
     mbar_init(&sh.end, 1);
     mbar_init(&sh.end2, 1);
-    sh.stop = 0;
+    sh.wait.stop = 0;
+    sh.wait.limit_us = a.waits.limit_us;
     fence_mbar_init();
   }
   if (warp == kScoreWarp) tmem_alloc(&sh.tmem, 512);
@@ -668,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto load = [&](const CUtensorMap* map, const int (&c)[4], bool in, int bytes) {
       if (turned) wait_or_stop(&sh.kv_empty[at.slot], at.turn ^ 1, sh, a.err);
       // (the whole warp or none of it: the lanes meet below)
-      if (__any_sync(kFull, *static_cast<volatile int*>(&sh.stop))) return;
+      if (__any_sync(kFull, *static_cast<volatile int*>(&sh.wait.stop))) return;
       if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[at.slot], bytes);
       __syncwarp();
       if (in)
@@ -678,6 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       at.step();
       if (!turned && ++issued == C::NS) turned = true;
     };
+    if (a.waits.stall) walk.left = 0;
     while (walk.next(s)) {
       for (int t = s.t0; t < s.t1; ++t) {
         const int tok = t * TN + box * p.box;

@@ -1167,7 +1167,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   cluster.barrier_arrive();  // (the wait is before the first word to another CTA)
   bool landed = true;
   if (p.bulk) {
-    if (tid == 0 && count > 0) {
+    if (tid == 0 && count > 0 && !p.waits.stall) {
       const uint32_t bytes = static_cast<uint32_t>(count) * sizeof(T);
       mbar_arrive_expect_tx(&sh.bar, bytes);
       const uint64_t pol = policy_evict_first();
@@ -1217,7 +1217,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     u = 0.0f;
   }
   if (k <= 0 || k >= p.V) k = 0;
-  if (p.bulk && count > 0) landed = wait_phase(&sh.bar, 0, kWaitNs);
+  if (p.bulk && count > 0) landed = wait_phase(&sh.bar, 0, p.waits.limit_us * 1000ull);
   if (!landed) wait_phase(&sh.bar, 0, kDrainNs);
   if (!mine_ok) {  // in every CTA of the cluster alike
     if (rank == 0 && tid == 0) raise_error(p.err, SD_DEV_ERR_CU_SEQLENS);

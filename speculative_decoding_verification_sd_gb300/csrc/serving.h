@@ -22,6 +22,13 @@ struct CacheView {
   int num_pages, page_size, max_pages, heads, dim;
 };
 
+// How long a wait on the device may last, and the test hook that makes it run out.
+constexpr uint32_t kWaitUs = 1000000;  // unless the caller sets one
+struct Waits {
+  uint32_t limit_us;
+  bool stall;
+};
+
 struct AppendParams {
   const uint16_t* k_new;
   const uint16_t* v_new;
@@ -46,6 +53,7 @@ struct AttendParams {
   uint16_t* out;
   float* lse;
   int* err;
+  Waits waits;
 };
 // The general kernel (any strides, page size and alignment), and the
 // tensor-core kernel; *taken = false when the cache's layout has no tensor map.
@@ -89,6 +97,7 @@ struct SampleParams {
   int* tokens;
   void* kept;
   int* err;
+  Waits waits;
   int slice;  // elements of a row per CTA (whole 16-byte vectors)
   bool bulk;  // rows start on 16 bytes and are whole vectors
   float2 t1[kExpTab], t2[kExpTab];  // 2^(-i/64), 2^(-i/4096) as (high, low) pairs

@@ -17,6 +17,18 @@ sd_status launched(cudaError_t e) {
                           : refuse(SD_ERR_CUDA, "%s: %s", cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
+// The options of the calls that have some.
+sd_status read_cfg(const sd_launch_cfg* cfg, sdk::Waits* w) {
+  *w = sdk::Waits{sdk::kWaitUs, false};
+  if (!cfg) return SD_OK;
+  if (cfg->blocks != 0 || cfg->wait_limit_us < 0 || cfg->reserved != 0)
+    return refuse(SD_ERR_INVALID_ARG, "sd_launch_cfg: blocks or reserved != 0, or a negative limit");
+  if (cfg->flags & ~SD_TEST_STALL) return refuse(SD_ERR_INVALID_ARG, "sd_launch_cfg: unknown flag bits 0x%x", cfg->flags);
+  w->stall = (cfg->flags & SD_TEST_STALL) != 0;
+  if (cfg->wait_limit_us > 0) w->limit_us = static_cast<uint32_t>(cfg->wait_limit_us);
+  return SD_OK;
+}
+
 // Checks of a cache and of the step's shape, common to append and attend.
 sd_status cache_checks(const sd_kv_cache* c, const int* cu_seqlens, const int* kv_lens, int bs,
                        int k_max, const int* err_flag, sdk::CacheView* view) {
@@ -87,6 +99,14 @@ sd_status sd_attend(const void* q, long long q_row_stride, int q_heads, const sd
                     const int* cu_seqlens, const int* kv_lens, int bs, int k_max, float scale,
                     void* out, float* lse_out, int* err_flag, void* workspace, size_t ws_bytes,
                     void* stream) {
+  return sd_attend_ex(q, q_row_stride, q_heads, cache, cu_seqlens, kv_lens, bs, k_max, scale, out, lse_out, err_flag,
+                      workspace, ws_bytes, nullptr, stream);
+}
+
+sd_status sd_attend_ex(const void* q, long long q_row_stride, int q_heads, const sd_kv_cache* cache,
+                       const int* cu_seqlens, const int* kv_lens, int bs, int k_max, float scale,
+                       void* out, float* lse_out, int* err_flag, void* workspace, size_t ws_bytes,
+                       const sd_launch_cfg* cfg, void* stream) {
   sdk::clear_last_error();
   sdk::AttendParams p{};
   const sd_status st = cache_checks(cache, cu_seqlens, kv_lens, bs, k_max, err_flag, &p.c);
@@ -112,6 +132,8 @@ sd_status sd_attend(const void* q, long long q_row_stride, int q_heads, const sd
   p.bs = bs;
   p.k_max = k_max;
   p.scale = scale;
+  const sd_status with = read_cfg(cfg, &p.waits);
+  if (with != SD_OK) return with;
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse_out;
   p.err = err_flag;
@@ -140,6 +162,14 @@ sd_status sd_sample(const void* logits, sd_dtype dt, int V, int rows, const int*
                     const float* temps, const int* top_k, const float* top_p, const float* min_p,
                     const float* uniforms, int* tokens, void* kept_out, int* err_flag,
                     void* stream) {
+  return sd_sample_ex(logits, dt, V, rows, cu_seqlens, bs, temps, top_k, top_p, min_p, uniforms, tokens, kept_out,
+                      err_flag, nullptr, stream);
+}
+
+sd_status sd_sample_ex(const void* logits, sd_dtype dt, int V, int rows, const int* cu_seqlens, int bs,
+                       const float* temps, const int* top_k, const float* top_p, const float* min_p,
+                       const float* uniforms, int* tokens, void* kept_out, int* err_flag,
+                       const sd_launch_cfg* cfg, void* stream) {
   sdk::clear_last_error();
   if (dt != SD_F32 && dt != SD_BF16) return refuse(SD_ERR_INVALID_ARG, "unknown dtype %d", static_cast<int>(dt));
   if (V < 1 || rows < 1) return refuse(SD_ERR_INVALID_ARG, "V=%d, rows=%d: need at least 1", V, rows);
@@ -156,6 +186,8 @@ sd_status sd_sample(const void* logits, sd_dtype dt, int V, int rows, const int*
   if (!aligned(logits, elem) || (kept_out && !aligned(kept_out, elem)))
     return refuse(SD_ERR_INVALID_ARG, "logits or kept_out not aligned to its elements");
   sdk::SampleParams p{};
+  const sd_status with = read_cfg(cfg, &p.waits);
+  if (with != SD_OK) return with;
   p.logits = logits;
   p.V = V;
   p.rows = rows;

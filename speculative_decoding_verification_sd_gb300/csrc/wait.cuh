@@ -5,8 +5,7 @@
 
 namespace sdk {
 
-constexpr uint64_t kWaitNs = 1000000000ull;       // a wait gives up after this time ...
-constexpr uint64_t kDrainNs = 2000000000ull;      // ... and a drain of copies in flight after this
+constexpr uint64_t kDrainNs = 2000000000ull;  // a drain of copies in flight gives up after this time
 
 __device__ __forceinline__ uint64_t clock_ns() {
   uint64_t t;

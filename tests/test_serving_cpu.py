@@ -144,3 +144,16 @@ def test_binding_refuses_what_does_not_fit(sd):
         sd.sample(z, t, kept=torch.zeros((2, 7)))
     with pytest.raises(ValueError):
         sd.sample(z.double(), t, kept=True)
+
+
+def test_options_refusals(sd):
+    lib = sd._lib.load()
+    nb = sd.sd_attend_workspace_bytes(4, 3, 16, 8, 64)
+    c = cache(sd)
+    for bad in ((1, 0, 0, 0), (-1, 0, 0, 0), (0, 0x1, 0, 0), (0, 0x40, 0, 0), (0, 0, -1, 0), (0, 0, 0, 1)):
+        cfg = ctypes.byref(sd.sd_launch_cfg(*bad))
+        assert lib.sd_attend_ex(P, 16 * 64, 16, ctypes.byref(c), P, P, 4, 3, 0.125, P, None, P, P, nb, cfg, 0) == \
+            sd.SD_ERR_INVALID_ARG, bad
+        assert lib.sd_sample_ex(P, sd.SD_BF16, 1024, 4, None, 4, P, None, None, None, P, P, None, P, cfg, 0) == \
+            sd.SD_ERR_INVALID_ARG, bad
+        assert b"sd_launch_cfg" in lib.sd_last_error_string()
