@@ -83,15 +83,27 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _torch_stream(stream):
+    if isinstance(stream, int):  # 0, and 1 by name: the default stream
+        return torch.cuda.default_stream() if stream in (0, 1) else torch.cuda.ExternalStream(stream)
+    return stream
+
+
 def _filling(stream):
     """Context in which torch allocates and fills on the stream that the call is given:
     fills are in order before the kernel, and memory that the call lets go of is handed
     out again behind it."""
-    if stream is None:
-        return contextlib.nullcontext()
-    if isinstance(stream, int):  # 0, and 1 by name: the default stream
-        stream = torch.cuda.default_stream() if stream in (0, 1) else torch.cuda.ExternalStream(stream)
-    return torch.cuda.stream(stream)
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(_torch_stream(stream))
+
+
+def _used_on(stream, *tensors):
+    """The caller's tensors may be freed on return: their memory is not handed out again
+    before the given stream has done the call."""
+    if stream is not None:
+        s = _torch_stream(stream)
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(s)
 
 
 def _dt(dt):
@@ -248,6 +260,7 @@ def plan(draft_lens: torch.Tensor, k_max: int, conf: Optional[torch.Tensor] = No
             budget_conf = torch.zeros(1, dtype=torch.float32, device=dev)
     sd_plan(conf, budget_conf, budget_draft_lens, bsb, draft_lens, bs, k_max, cost,
             0 if cost is None else cost.numel(), T, mode, B, mask, nv, cu, err, None, 0, stream)
+    _used_on(stream, draft_lens, conf, cost, budget_conf, budget_draft_lens, err)
     return PlanResult(B, mask[:, :k_max], nv, cu, err)
 
 
@@ -268,6 +281,7 @@ def verify(target: torch.Tensor, draft: Optional[torch.Tensor], dt, V: int,
             workspace = verify_workspace(bs, k_max, V, dt, dev)
     sd_verify_ex(target, draft, dt, V, draft_ids, uniforms, temps, cu_seqlens, bs, k_max, acc,
                  out, pr, err, workspace, workspace.numel(), cfg=cfg, stream=stream)
+    _used_on(stream, target, draft, draft_ids, uniforms, temps, cu_seqlens, err, workspace)
     return VerifyResult(acc, out, pr, err)
 
 
@@ -315,6 +329,9 @@ class KVCache:
                              _ptr(v_scale), k.stride(0), k.stride(1), k.stride(2), self.dt,
                              self.num_pages, self.page_size, page_table.shape[1], self.heads,
                              self.head_dim)
+
+    def tensors(self):
+        return self.k, self.v, self.page_table, self.k_scale, self.v_scale
 
 
 def _cache(cache):
@@ -439,6 +456,7 @@ def append(k_new: torch.Tensor, v_new: torch.Tensor, cache: KVCache, cu_seqlens:
         with _filling(stream):
             err = torch.zeros(1, dtype=torch.int32, device=cache.k.device)
     sd_cache_append(ka, va, ks, cache, cu_seqlens, kv_lens, bs, k_max, err, stream)
+    _used_on(stream, k_new, v_new, cu_seqlens, kv_lens, err, *cache.tensors())
     return err
 
 
@@ -476,6 +494,7 @@ def attend(q: torch.Tensor, cache: KVCache, cu_seqlens: torch.Tensor, kv_lens: t
     sd_attend(qa, qs, q_heads, cache, cu_seqlens, kv_lens, bs, k_max,
               dim ** -0.5 if scale is None else scale, out, lse, err, workspace, workspace.numel(),
               stream)
+    _used_on(stream, q, cu_seqlens, kv_lens, out, lse, err, workspace, *cache.tensors())
     return AttendResult(out, lse, err)
 
 
@@ -516,4 +535,5 @@ def sample(logits: torch.Tensor, temps: torch.Tensor, uniforms: Optional[torch.T
         raise ValueError("kept must have the logits' shape and dtype")
     sd_sample(logits, logits.dtype, V, rows, cu_seqlens, bs, temps, top_k, top_p, min_p, uniforms,
               tokens, kept, err, stream)
+    _used_on(stream, logits, temps, uniforms, top_k, top_p, min_p, cu_seqlens, tokens, kept, err)
     return SampleResult(tokens, kept, err)

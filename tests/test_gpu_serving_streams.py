@@ -128,6 +128,35 @@ def test_verify_fills_on_the_calls_stream(side):
     assert torch.equal(torch.nan_to_num(r.probs), torch.nan_to_num(want.probs)) and int(r.err) == 0
 
 
+def test_inputs_may_be_freed_on_return(side):
+    """The memory of an input that the caller lets go of is not handed out again before
+    the call's stream has read it."""
+    s, arg = side
+    q, cache, cu, lens, k_max = attend_inputs()
+    g = torch.Generator().manual_seed(6)
+    z, t, u = torch.randn((300, 5000), generator=g).cuda(), torch.ones(300).cuda(), torch.rand(300, generator=g).cuda()
+    new = torch.randn((24, 2, 128), generator=g).bfloat16().cuda()
+    err = i32([0])
+    sd.append(new, new, cache, cu, lens, k_max)
+    want, wanted = sd.attend(q, cache, cu, lens, k_max), sd.sample(z, t, u)
+    k = cache.k.clone()
+    cache.k.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        hold()
+    sd.append(new.clone(), new.clone(), cache, cu, lens, k_max, stream=arg)
+    junk = [torch.full_like(new, 7.0) for _ in range(4)]
+    with torch.cuda.stream(s):
+        cache.k.copy_(k)
+    r = sd.attend(q.clone(), cache, cu, lens, k_max, err=err, stream=arg)
+    junk += [torch.full_like(q, 7.0) for _ in range(4)]
+    d = sd.sample(z.clone(), t, u, stream=arg)
+    junk += [torch.full_like(z, 7.0) for _ in range(2)]
+    torch.cuda.synchronize()
+    assert torch.equal(r.out, want.out) and int(err) == 0 and torch.equal(d.tokens, wanted.tokens)
+    assert all(bool((x == 7.0).all()) for x in junk)
+
+
 def both(*work, times):
     """Runs the functions in a thread each, on streams of their own; raises what one of them raised."""
     failed, ready = [], threading.Barrier(len(work))
