@@ -679,7 +679,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (in)
         tma_load_4d(ring + at.slot * C::SLOT + blk * (TN * 128) + box * p.box * 128, map, c[0], c[1], c[2], c[3],
                     &sh.kv_full[at.slot], pol);
-      __syncwarp();
       at.step();
       if (!turned && ++issued == C::NS) turned = true;
     };
