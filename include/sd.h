@@ -399,6 +399,8 @@ typedef struct {
  *                  (its rows are not written); SD_DEV_ERR_CACHE: a position
  *                  outside [0, max_pages * page_size) or a page id outside
  *                  [0, num_pages) (that row is not written).
+ * A prompt longer than 16 tokens goes in as several requests of one call, each
+ * with the prompt's row of the page table and kv_lens at the end of its rows.
  * Rows that name the same cache slot (a page shared by two requests) race;
  * shared pages must be read-only, as in a prefix cache.
  * Limits: 1 <= bs <= SD_MAX_VERIFY_BS, bs * (k_max + 1) rows, 0 <= k_max <=
@@ -435,6 +437,9 @@ sd_status sd_cache_append(const void* k_new, const void* v_new, long long row_st
  * takes nothing from tokens that it does not see: a non-finite key or value of
  * a late token of the step leaves the rows before it as they are.  Results do not depend on timing: partial
  * sums are joined in a fixed order.
+ * Two kernels: caches whose bases, strides and q_row_stride are multiples of 16
+ * bytes, with pages of a multiple of 8 tokens, are read by the tensor-core one;
+ * any other layout by one that takes some ten times as long.
  * Limits: as sd_cache_append, q_heads a multiple of heads, q_heads / heads <= SD_MAX_HEAD_GROUP, |scale| finite. */
 #define SD_MAX_HEAD_GROUP 128
 size_t sd_attend_workspace_bytes(int bs, int k_max, int q_heads, int heads, int head_dim);

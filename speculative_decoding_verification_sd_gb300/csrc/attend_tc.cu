@@ -26,10 +26,9 @@
 // cache, whose softmax costs most, 64 rows or fewer are laid out twice and each
 // copy weighs its own half of the tile's tokens (zeros elsewhere): independent
 // partial sums, joined at the segment's end, for which all softmax warps work.
-// 256 requests of up to 64 rows take 151 us with two copies, 160 with one and 157
-// with up to four; 19 of 65536 tokens and 4 rows 466, 511 and 457.  Over a bf16
-// cache the bytes hide the softmax and one copy is best (64 ragged single rows
-// 106 us, with two 113).
+// 256 requests of up to 64 rows take 169 us with two copies, 184 with one; 19 of
+// 65536 tokens and 4 rows 495 and 547; but 64 ragged single rows 99 and 89.  Over a
+// bf16 cache the bytes hide the softmax, and there is one copy.
 //
 // Softmax.  Running maximum and sum per lane, fp32.  O is rescaled only when
 // the maximum has grown by more than 2^SLACK since O's reference; until
@@ -50,15 +49,15 @@
 // of the terms accumulate in the same fp32 accumulators.
 //
 // What bounds it.  The cache's bytes over a bf16 cache: 19 requests of 65536
-// tokens (5.1 GB) take 750 us, 6.8 TB/s, the copy rate, whatever the rows.  Over
-// an 8-bit cache a tile's 20 tensor instructions take 1280 cycles, its bytes 1400
-// at the copy rate, and the chain scores, softmax, weights, O shows between them:
-// 5.4 TB/s with 4 rows, 5.0 with 64, 4.2 with 128.  Short segments cost more than
+// tokens (5.1 GB) take 744 us with up to 64 rows and 761 with 128, 6.7 to 6.9 TB/s,
+// the copy rate.  Over an 8-bit cache a tile's 20 tensor instructions take 1280
+// cycles, its bytes 1400 at the copy rate, and the chain scores, softmax, weights, O
+// shows between them: 5.3 TB/s with 4 rows, 5.1 with 64, 4.2 with 128.  Short segments cost more than
 // their tiles: rows in, O out, parts joined, all by warps 8-11 while the next
 // segment runs.  What those warps wait for is mostly instructions (the softmax
 // warps' code passes through the same caches), so their loops are short, waits
 // that do not end at once are out of line, and the softmax is unrolled no further
-// than its registers ask for (a step over an 8-bit cache 193 -> 153 us).
+// than its registers ask for (that took a step over an 8-bit cache from 193 to 153 us).
 //
 // Every wait is bounded; one that gives up raises SD_DEV_ERR_TIMEOUT and lets the
 // CTA run to its end without waiting.
@@ -86,15 +85,15 @@ struct Cfg {
   // Words that O passes through on its way out: 128 lanes of 32 columns, each
   // shifted by 16 bytes in the banks; of all 128 columns where the small tiles of
   // an 8-bit cache leave room, so that O is free for the next segment at once
-  // (159 us; through 32 columns at a time 167)
+  // (169 us; through 32 columns at a time 173)
   static constexpr int STAGE_WORDS = 128 * (F8 && DP == 128 ? 132 : 36);
   static constexpr int STAGE = STAGE_WORDS * 4;
   static constexpr int QROW = DP * 2 + 16;             // bytes of a fetched query row, shifted in the banks
   static constexpr int QRAW = 128 * QROW;
   static constexpr int TAIL = 10240;                   // Shared, and the base's alignment
   // Tiles' time that a segment costs besides its tiles.  A step over an 8-bit
-  // cache: 163 us with 2, 159 with 3, 159 with 4; a ragged one over a bf16 cache
-  // 116 with 1, 119 with 2.
+  // cache: 171 us with 2, 169 with 3, 175 with 4; a ragged one over a bf16 cache
+  // 106 with 1, 112 with 2.
   static constexpr int LEAD = SLOT >= 32768 ? 1 : 3;
   static constexpr int FIT = (232448 - STAGE - QRAW - TAIL) / SLOT;
   static constexpr int NS = FIT < kMaxSlots ? FIT : kMaxSlots;
@@ -464,7 +463,7 @@ __device__ __noinline__ bool clean_values(unsigned char* v, int by_all, int used
 // the step's own tokens that they see, which clean_values has taken out of the tiles
 // (a positive weight times such a value is that value).  Out of line and after the
 // rows are out: few calls have such values, and what stands within the rows' way
-// out costs every call (a step over an 8-bit cache 164 us, with a branch there 176).
+// out costs every call (a step over an 8-bit cache 164 us, with a call there 176).
 template <bool F8, int NBLK>
 __device__ __noinline__ void add_not_finite(const Params& p, const Seg s, bool whole, long long part_row, int tid) {
   using C = Cfg<F8, NBLK>;

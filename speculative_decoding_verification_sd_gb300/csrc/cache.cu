@@ -10,7 +10,8 @@
 // issue slots, hence packed quotients and no integer division.  4700 rows of 8
 // heads of 128 into an 8-bit cache (28 MB in and out) take 9.6 us, 2.9 TB/s of
 // the copy's 6.8; a launch with next to nothing to do 2.  Rows, bases or strides
-// off 16 bytes go element by element (8-bit cache 17 us for 15, bf16 29 for 13).
+// off 16 bytes go element by element: 2 us more for those rows into an 8-bit cache,
+// twice the time into a bf16 one (32 us for 15, with what a launch costs).
 #include "cache.cuh"
 #include "f32x2.cuh"
 

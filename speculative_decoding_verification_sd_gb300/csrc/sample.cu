@@ -43,7 +43,7 @@
 // and the cluster's barriers between them), a top-k of 50 20, a top-p alone 40
 // (11 of them the weights of all tokens) and a top-k of 5000 33: chains of short
 // phases that two CTAs an SM overlap only in part.  1201 rows of all kinds in
-// 362 us are 1.65 TB/s, a quarter of the copy rate.
+// 366 us are 1.63 TB/s, a quarter of the copy rate.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -183,7 +183,6 @@ struct Shared {
   uint32_t bin, bin_n, base_c;
   u64 base_m;
   uint32_t cut_key, cut_idx;
-  u64 cut_m;
 };
 
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer in the low bits
@@ -1455,9 +1454,9 @@ template <typename T>
 cudaError_t launch(SampleParams& p, cudaStream_t s) {
   constexpr int N = Elem<T>::N;
   const int vecs = (p.V + N - 1) / N;
-  // Slices of up to 66 KB, so that two CTAs share an SM: a step's 1201 truncated
-  // rows of 129280 take 380 us, with slices of 132 KB 383, of 34 KB 664; 256 mixed
-  // rows 127, 146 and 168.
+  // Slices of up to 66 KB, so that two CTAs share an SM: when a step's 1201
+  // truncated rows of 129280 took 380 us, they took 383 with slices of 132 KB and
+  // 664 with 34 KB; 256 mixed rows 127, 146 and 168.
   int C = 1;
   while (C < 8 && (vecs + C - 1) / C * 16 > 66 * 1024) C *= 2;
   // few rows: more CTAs a row, while a thread still has a vector (4 rows of 129280

@@ -248,3 +248,28 @@ def test_sample_leaves_every_row_of_an_invalid_range_alone():
         live = [2] if cu == [4, 2, 3] else []
         rest = [row for row in range(8) if row not in live]
         assert bool((kept[rest] == 77.0).all()) and bool((tokens[rest] == -5).all())
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("page", [16, 24, 5])
+def test_a_prompt_goes_in_as_requests_that_share_its_pages(page, e4m3):
+    g = torch.Generator().manual_seed(8)
+    heads, dim, tokens = 2, 64, 100
+    k, v, table, ks, vs = ref.make_cache(g, [tokens], page, heads, dim, e4m3)
+    new = torch.randn((112, 2, heads, dim), generator=g).bfloat16()
+    counts = [16] * 6 + [4]
+    cache = device_cache(k, v, table.repeat(7, 1), ks, vs)
+    nd = new.cuda()
+    ends = torch.tensor(counts).cumsum(0).tolist()
+    err = sd.append(nd[:, 0], nd[:, 1], cache, torch.tensor(ref.compaction(counts)).cuda(), i32(ends), 15)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    t = torch.arange(tokens)
+    at = table[0, t // page].long(), t % page
+    for w, (x, sc) in enumerate(((k, ks), (v, vs))):
+        y = new[:tokens, w]
+        y = (y.float() / sc[:, None]).clamp(-448, 448).to(x.dtype) if e4m3 else y
+        for i in range(tokens):
+            x[at[0][i], at[1][i]] = y[i]
+        got = (cache.v if w else cache.k).cpu()
+        assert torch.equal(got.view(torch.uint8), x.contiguous().view(torch.uint8))
