@@ -218,3 +218,24 @@ def test_threads_attend_with_a_workspace_each():
     both(a[0], b[0], times=300)
     for _, got, want, err in (a, b):
         assert torch.equal(got, want) and int(err) == 0
+
+
+def test_a_captured_call_may_name_its_stream():
+    """With nothing handed over, and the capturing stream given as a handle."""
+    q, cache, cu, lens, k_max = attend_inputs()
+    z = torch.randn((9, 5000), generator=torch.Generator().manual_seed(1)).cuda()
+    t, u = torch.ones(9).cuda(), torch.linspace(0.0, 0.9, 9).cuda()
+    want, wanted = sd.attend(q, cache, cu, lens, k_max, lse=True), sd.sample(z, t, u, kept=True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        at = torch.cuda.current_stream().cuda_stream
+        r = sd.attend(q, cache, cu, lens, k_max, lse=True, stream=at)
+        d = sd.sample(z, t, u, kept=True, stream=at)
+    for _ in range(2):
+        for x in (r.out, r.lse, d.tokens, d.kept):
+            x.fill_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(r.out, want.out) and torch.equal(r.lse, want.lse) and int(r.err) == 0
+        assert torch.equal(d.tokens, wanted.tokens) and torch.equal(d.kept, wanted.kept) and int(d.err) == 0
