@@ -89,21 +89,23 @@ def _torch_stream(stream):
     return stream
 
 
+_CURRENT = contextlib.nullcontext()  # (made once: a call takes 8 us in all)
+
+
 def _filling(stream):
     """Context in which torch allocates and fills on the stream that the call is given:
     fills are in order before the kernel, and memory that the call lets go of is handed
     out again behind it."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(_torch_stream(stream))
+    return _CURRENT if stream is None else torch.cuda.stream(_torch_stream(stream))
 
 
 def _used_on(stream, *tensors):
     """The caller's tensors may be freed on return: their memory is not handed out again
     before the given stream has done the call."""
-    if stream is not None:
-        s = _torch_stream(stream)
-        for t in tensors:
-            if isinstance(t, torch.Tensor) and t.is_cuda:
-                t.record_stream(s)
+    s = _torch_stream(stream)
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(s)
 
 
 def _dt(dt):
@@ -260,7 +262,8 @@ def plan(draft_lens: torch.Tensor, k_max: int, conf: Optional[torch.Tensor] = No
             budget_conf = torch.zeros(1, dtype=torch.float32, device=dev)
     sd_plan(conf, budget_conf, budget_draft_lens, bsb, draft_lens, bs, k_max, cost,
             0 if cost is None else cost.numel(), T, mode, B, mask, nv, cu, err, None, 0, stream)
-    _used_on(stream, draft_lens, conf, cost, budget_conf, budget_draft_lens, err)
+    if stream is not None:
+        _used_on(stream, draft_lens, conf, cost, budget_conf, budget_draft_lens, err)
     return PlanResult(B, mask[:, :k_max], nv, cu, err)
 
 
@@ -281,7 +284,8 @@ def verify(target: torch.Tensor, draft: Optional[torch.Tensor], dt, V: int,
             workspace = verify_workspace(bs, k_max, V, dt, dev)
     sd_verify_ex(target, draft, dt, V, draft_ids, uniforms, temps, cu_seqlens, bs, k_max, acc,
                  out, pr, err, workspace, workspace.numel(), cfg=cfg, stream=stream)
-    _used_on(stream, target, draft, draft_ids, uniforms, temps, cu_seqlens, err, workspace)
+    if stream is not None:
+        _used_on(stream, target, draft, draft_ids, uniforms, temps, cu_seqlens, err, workspace)
     return VerifyResult(acc, out, pr, err)
 
 
@@ -456,7 +460,8 @@ def append(k_new: torch.Tensor, v_new: torch.Tensor, cache: KVCache, cu_seqlens:
         with _filling(stream):
             err = torch.zeros(1, dtype=torch.int32, device=cache.k.device)
     sd_cache_append(ka, va, ks, cache, cu_seqlens, kv_lens, bs, k_max, err, stream)
-    _used_on(stream, k_new, v_new, cu_seqlens, kv_lens, err, *cache.tensors())
+    if stream is not None:
+        _used_on(stream, k_new, v_new, cu_seqlens, kv_lens, err, *cache.tensors())
     return err
 
 
@@ -494,7 +499,8 @@ def attend(q: torch.Tensor, cache: KVCache, cu_seqlens: torch.Tensor, kv_lens: t
     sd_attend(qa, qs, q_heads, cache, cu_seqlens, kv_lens, bs, k_max,
               dim ** -0.5 if scale is None else scale, out, lse, err, workspace, workspace.numel(),
               stream)
-    _used_on(stream, q, cu_seqlens, kv_lens, out, lse, err, workspace, *cache.tensors())
+    if stream is not None:
+        _used_on(stream, q, cu_seqlens, kv_lens, out, lse, err, workspace, *cache.tensors())
     return AttendResult(out, lse, err)
 
 
@@ -535,5 +541,6 @@ def sample(logits: torch.Tensor, temps: torch.Tensor, uniforms: Optional[torch.T
         raise ValueError("kept must have the logits' shape and dtype")
     sd_sample(logits, logits.dtype, V, rows, cu_seqlens, bs, temps, top_k, top_p, min_p, uniforms,
               tokens, kept, err, stream)
-    _used_on(stream, logits, temps, uniforms, top_k, top_p, min_p, cu_seqlens, tokens, kept, err)
+    if stream is not None:
+        _used_on(stream, logits, temps, uniforms, top_k, top_p, min_p, cu_seqlens, tokens, kept, err)
     return SampleResult(tokens, kept, err)
